@@ -7,8 +7,8 @@ namespace sg {
 namespace w4 {
 // Rows of weights that start on 16 bytes, on 4, anywhere.
 template <typename X>
-using Run = int(const X* x, const X* scales, X* y, Params p, int group, int sms, cudaMemPool_t pool,
-                cudaStream_t stream);
+using Run = int(const X* x, const X* scales, X* y, Params p, int group, const DeviceInfo* dev,
+                cudaMemPool_t pool, cudaStream_t stream);
 Run<float> run_f32, run_f32_words, run_f32_bytes;
 Run<__nv_bfloat16> run_bf16, run_bf16_words, run_bf16_bytes;
 
@@ -100,10 +100,10 @@ extern "C" int sgemv_w4(int type, int64_t pairs, int64_t repeat, int64_t N, int6
     if (type == SGEMM_TYPE_BF16) {
         constexpr Run<__nv_bfloat16>* RUNS[3] = {run_bf16, run_bf16_words, run_bf16_bytes};
         return RUNS[place](static_cast<const __nv_bfloat16*>(X), static_cast<const __nv_bfloat16*>(scales),
-                           static_cast<__nv_bfloat16*>(Y), p, static_cast<int>(group), dev->sm_count, pool,
+                           static_cast<__nv_bfloat16*>(Y), p, static_cast<int>(group), dev, pool,
                            stream);
     }
     constexpr Run<float>* RUNS[3] = {run_f32, run_f32_words, run_f32_bytes};
     return RUNS[place](static_cast<const float*>(X), static_cast<const float*>(scales),
-                       static_cast<float*>(Y), p, static_cast<int>(group), dev->sm_count, pool, stream);
+                       static_cast<float*>(Y), p, static_cast<int>(group), dev, pool, stream);
 }

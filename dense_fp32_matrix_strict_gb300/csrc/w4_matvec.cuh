@@ -29,6 +29,7 @@
 // not matter to the sum.
 #pragma once
 
+#include <atomic>
 #include <cstring>
 
 #include "expert.h"
@@ -551,21 +552,36 @@ __global__ void __launch_bounds__(32 * WARPS, 1) w4_kernel(const X* __restrict__
 template <typename X>
 using Kernel = void (*)(const X*, const X*, X*, Params);
 
+// Sets *kernel, allowed all of an SM's shared memory. The limit belongs to the
+// function, not to a launch: it is set once per device and to one size, so that
+// host threads whose calls need different amounts cannot take it from one
+// another.
+template <typename X, int NT, int GROUP, int WARPS, bool ZEROS, int ALIGN>
+cudaError_t prepare(int device, Kernel<X>* kernel) {
+    static std::atomic<bool> ready[64] = {};           // (device_info admits indexes below 64)
+    *kernel = &w4_kernel<X, NT, GROUP, WARPS, ZEROS, ALIGN>;
+    if (ready[device].load(std::memory_order_acquire)) return cudaSuccess;
+    const cudaError_t e =
+        cudaFuncSetAttribute(*kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, MAX_SMEM);
+    if (e == cudaSuccess) ready[device].store(true, std::memory_order_release);
+    return e;
+}
+
 template <typename X, int NT, int WARPS, bool ZEROS, int ALIGN>
-Kernel<X> pick_group(int group) {
-    return group == 32   ? &w4_kernel<X, NT, 32, WARPS, ZEROS, ALIGN>
-           : group == 64 ? &w4_kernel<X, NT, 64, WARPS, ZEROS, ALIGN>
-                         : &w4_kernel<X, NT, 128, WARPS, ZEROS, ALIGN>;
+cudaError_t pick_group(int group, int device, Kernel<X>* kernel) {
+    return group == 32   ? prepare<X, NT, 32, WARPS, ZEROS, ALIGN>(device, kernel)
+           : group == 64 ? prepare<X, NT, 64, WARPS, ZEROS, ALIGN>(device, kernel)
+                         : prepare<X, NT, 128, WARPS, ZEROS, ALIGN>(device, kernel);
 }
 
 template <typename X, bool ZEROS, int ALIGN>
-Kernel<X> pick(bool wide, int64_t cols, int group) {
+cudaError_t pick(bool wide, int64_t cols, int group, int device, Kernel<X>* kernel) {
     if (wide)
-        return cols <= 8 ? pick_group<X, 1, 16, ZEROS, ALIGN>(group)
-                         : pick_group<X, 2, 16, ZEROS, ALIGN>(group);
-    return cols <= 8    ? pick_group<X, 1, 8, ZEROS, ALIGN>(group)
-           : cols <= 16 ? pick_group<X, 2, 8, ZEROS, ALIGN>(group)
-                        : pick_group<X, 4, 8, ZEROS, ALIGN>(group);
+        return cols <= 8 ? pick_group<X, 1, 16, ZEROS, ALIGN>(group, device, kernel)
+                         : pick_group<X, 2, 16, ZEROS, ALIGN>(group, device, kernel);
+    return cols <= 8    ? pick_group<X, 1, 8, ZEROS, ALIGN>(group, device, kernel)
+           : cols <= 16 ? pick_group<X, 2, 8, ZEROS, ALIGN>(group, device, kernel)
+                        : pick_group<X, 4, 8, ZEROS, ALIGN>(group, device, kernel);
 }
 
 // y = the slabs' sums, in order.
@@ -591,9 +607,10 @@ __global__ void __launch_bounds__(256) join_kernel(const Params p, X* __restrict
 // kernel (10 float tokens, 6720 x 6184: 40 us when this came; three tokens at a
 // time with all of k took 82).
 template <typename X, int ALIGN>
-int run(const X* x, const X* scales, X* y, Params p, int group, int sms, cudaMemPool_t pool,
-        cudaStream_t stream) {
+int run(const X* x, const X* scales, X* y, Params p, int group, const DeviceInfo* dev,
+        cudaMemPool_t pool, cudaStream_t stream) {
     constexpr int PIECES = sizeof(X) == 4 ? 3 : 1;
+    const int sms = dev->sm_count;
     const int slot = slot_bytes(sizeof(X), group, ALIGN);
     auto need = [&](int warps, int stages, int64_t cols, int64_t units) {
         return static_cast<int64_t>(warps) * stages * slot + cols * ((units * UNIT_K + 32) * 2 + warps * 128);
@@ -656,10 +673,10 @@ int run(const X* x, const X* scales, X* y, Params p, int group, int sms, cudaMem
         }
     }
     p.ws = static_cast<float*>(ws);
-    Kernel<X> kernel = p.zeros != nullptr ? pick<X, true, ALIGN>(wide, cols, group)
-                                          : pick<X, false, ALIGN>(wide, cols, group);
+    Kernel<X> kernel = nullptr;
+    e = p.zeros != nullptr ? pick<X, true, ALIGN>(wide, cols, group, dev->device, &kernel)
+                           : pick<X, false, ALIGN>(wide, cols, group, dev->device, &kernel);
     const size_t smem = static_cast<size_t>(need(warps, p.stages, cols, p.slab));
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e == cudaSuccess)
         e = launch_kernel(kernel,
                           dim3(static_cast<unsigned>(gx), static_cast<unsigned>(chunks),

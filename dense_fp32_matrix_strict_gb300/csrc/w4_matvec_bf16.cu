@@ -4,9 +4,9 @@
 namespace sg {
 namespace w4 {
 
-int run_bf16(const __nv_bfloat16* x, const __nv_bfloat16* scales, __nv_bfloat16* y, Params p, int group, int sms,
-            cudaMemPool_t pool, cudaStream_t stream) {
-    return run<__nv_bfloat16, 16>(x, scales, y, p, group, sms, pool, stream);
+int run_bf16(const __nv_bfloat16* x, const __nv_bfloat16* scales, __nv_bfloat16* y, Params p, int group,
+            const DeviceInfo* dev, cudaMemPool_t pool, cudaStream_t stream) {
+    return run<__nv_bfloat16, 16>(x, scales, y, p, group, dev, pool, stream);
 }
 
 }  // namespace w4

@@ -4,9 +4,9 @@
 namespace sg {
 namespace w4 {
 
-int run_f32(const float* x, const float* scales, float* y, Params p, int group, int sms,
-            cudaMemPool_t pool, cudaStream_t stream) {
-    return run<float, 16>(x, scales, y, p, group, sms, pool, stream);
+int run_f32(const float* x, const float* scales, float* y, Params p, int group,
+            const DeviceInfo* dev, cudaMemPool_t pool, cudaStream_t stream) {
+    return run<float, 16>(x, scales, y, p, group, dev, pool, stream);
 }
 
 }  // namespace w4

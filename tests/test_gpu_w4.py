@@ -215,3 +215,72 @@ def test_few_rows_of_long_inputs(tokens, N, K, dtype):
     x, q, s, z = make(tokens, N, K, 128, dtype, False)
     y = call(x, q, s, z, 128, K, N)
     assert close(y, *reference(x, q, s, z, 128, K), dtype, K)
+
+
+# Calls one entry point `loops` times from each of `n` threads without
+# Python's lock between them; returns how many calls were refused.
+CALLER = r"""
+#include <pthread.h>
+#include <stdint.h>
+typedef int (*Entry)(int, int64_t, int64_t, int64_t, int64_t, int64_t, const void*, int64_t, const void*, int64_t,
+                     int64_t, const void*, const void*, int64_t, const void*, void*, int64_t, void*);
+struct Args { int64_t K; const void *x, *q, *s; void *y, *stream; };
+static Entry entry;
+static int loops, rows, group;
+static pthread_barrier_t start;
+static void* work(void* arg) {
+    const struct Args* a = arg;
+    intptr_t refused = 0;
+    pthread_barrier_wait(&start);
+    for (int i = 0; i < loops; ++i)
+        refused += entry(1, 1, 1, rows, a->K, group, a->x, a->K, a->q, a->K / 2, 0, a->s, 0, 1, 0, a->y, rows,
+                         a->stream) != 0;
+    return (void*)refused;
+}
+int call_from_threads(void* fn, int n, int times, int N, int per, const struct Args* args) {
+    pthread_t threads[16];
+    int refused = 0;
+    entry = (Entry)fn; loops = times; rows = N; group = per;
+    pthread_barrier_init(&start, 0, n);
+    for (int i = 0; i < n; ++i) pthread_create(&threads[i], 0, work, (void*)&args[i]);
+    for (int i = 0; i < n; ++i) {
+        void* r;
+        pthread_join(threads[i], &r);
+        refused += (int)(intptr_t)r;
+    }
+    pthread_barrier_destroy(&start);
+    return refused;
+}
+"""
+
+
+def test_host_threads_call_concurrently(tmp_path):
+    # Threads whose calls need different amounts of shared memory of the same
+    # kernel: no call is refused for another's sake, and each gets its result.
+    import ctypes
+    import subprocess
+    torch = _torch()
+    (tmp_path / "caller.c").write_text(CALLER)
+    subprocess.run(["gcc", "-O1", "-shared", "-fPIC", "-pthread", "-o", str(tmp_path / "caller.so"),
+                    str(tmp_path / "caller.c")], check=True)
+    caller = ctypes.CDLL(str(tmp_path / "caller.so"))
+
+    class Args(ctypes.Structure):
+        _fields_ = [("K", ctypes.c_int64)] + [(n, ctypes.c_void_p) for n in ("x", "q", "s", "y", "stream")]
+
+    N, group, kept = 48, 128, []
+    sizes = (512, 1024, 4096, 6144)
+    args = (Args * len(sizes))()
+    for i, K in enumerate(sizes):
+        x, q, s, _ = make(1, N, K, group, torch.bfloat16, False, seed=i)
+        want = call(x, q, s, None, group, K, N).contiguous()
+        x, q, s, y, stream = x.cuda(), q.cuda(), s.cuda(), torch.empty_like(want), torch.cuda.Stream()
+        args[i] = Args(K, x.data_ptr(), q.data_ptr(), s.data_ptr(), y.data_ptr(), stream.cuda_stream)
+        kept.append((x, q, s, y, stream, want))
+    torch.cuda.synchronize()
+    entry = ctypes.cast(sg.load().sgemv_w4, ctypes.c_void_p)
+    assert caller.call_from_threads(entry, len(sizes), 2000, N, group, args) == 0
+    sg.check_status()
+    torch.cuda.synchronize()
+    for x, q, s, y, stream, want in kept:
+        assert torch.equal(y, want)
