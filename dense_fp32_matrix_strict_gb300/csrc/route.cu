@@ -382,6 +382,8 @@ __global__ void __launch_bounds__(THREADS) route_place_kernel(const Params p) {
 // over all experts, or (renorm) over the chosen ones and 0 elsewhere, and
 // s = sum_j dw_j p[e_j],
 //     dl[e] = p[e] * ((dw_j if e = e_j else 0) - s).
+// A choice without an expert, or whose logit is -inf or NaN, takes no part: its
+// dw_j may be NaN.
 // One warp per token, the probabilities recomputed from the logits; reads the
 // logits once and writes the gradient once: bandwidth bound.
 constexpr int BWD_WARPS = 8;
@@ -412,6 +414,7 @@ route_backward_kernel(const L* __restrict__ logits, const int64_t T, const int E
         // The chosen logits, and for the softmax over all the others too.
         const float own = my_expert >= 0 ? load_f32(row + my_expert) : -INFINITY;
         const bool able = own > -INFINITY;                // not -inf, not NaN
+        if (!able) dw = 0.0f;                             // no expert: anything may stand there
         if (!renorm) {
 #pragma unroll
             for (int h = 0; h < VPL / 4; ++h) {

@@ -531,6 +531,8 @@ SGEMM_API int sgemm_route(int type, int64_t T, int64_t E, int64_t top, int renor
  * weights' softmax (over all experts, or with renorm 1 over the chosen ones)
  * and s = sum_j dweights[j] p[experts[j]],
  *     dlogits[e] = p[e] * ((dweights[j] if e == experts[j], else 0) - s).
+ * The dweights of a choice without an expert, or whose logit is -inf or NaN,
+ * are not used and may hold anything.
  * dlogits is T x E of `type` with row stride ldd and is written whole.
  */
 SGEMM_API int sgemm_route_backward(int type, int64_t T, int64_t E, int64_t top, int renorm,

@@ -228,3 +228,56 @@ def test_many_equal_logits(T, E, top):
     for renorm in (True, False):
         _, got, _ = route(logits, top, renorm)
         check_forward(got, plain(logits.numpy(), top, renorm))
+
+
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("T", [40, 700])
+def test_weight_gradients_of_choices_without_an_expert_are_not_used(T, dtype, renorm):
+    # No row stands behind such a choice, so what a caller has there may be
+    # anything: the other choices' gradients are those of the formula.
+    torch = _torch()
+    dt = getattr(torch, dtype)
+    E, top = 30, 6
+    g = torch.Generator().manual_seed(T)
+    logits = torch.randn(T, E, generator=g).to(dt)
+    logits[torch.rand(T, E, generator=g) < 0.85] = float("-inf")
+    logits[::9] = float("-inf")
+    dev, got, raw = route(logits, top, renorm)
+    want = plain(logits.float().numpy(), top, renorm)
+    none = torch.from_numpy(want[1] < 0)
+    assert bool(none.any()) and not bool(none.all())
+    dw = torch.randn(T, top, generator=g)
+    d = np.where(none, 0.0, dw.numpy().astype(np.float64))
+    s = (d * want[0]).sum(1, keepdims=True)
+    up = np.zeros_like(want[5])
+    for t in range(T):
+        for j in range(top):
+            if want[1][t, j] >= 0:
+                up[t, want[1][t, j]] = d[t, j]
+    ref = want[5] * (up - s)
+    # As for the gradient of the formula above: p, s and the output's rounding.
+    size = want[5] * (np.abs(d).max() * 2)
+    tol = (200 + E) * 2.0 ** -24 * size + (2.0 ** -8 * np.abs(ref) if dtype == "bfloat16" else 0) + 1e-37
+    for bad in (float("nan"), float("inf"), float("-inf")):
+        dl = torch.full((T, E), 9.0, dtype=dt, device="cuda")
+        sg.sgemm_route_backward_tensors(dev, raw["experts"], dw.masked_fill(none, bad).cuda(), dl, renorm=renorm)
+        sg.check_status()
+        assert np.all(np.abs(dl.float().cpu().numpy() - ref) <= tol)
+
+
+@pytest.mark.parametrize("renorm", [True, False])
+def test_weight_gradient_of_a_masked_logit_is_not_used(renorm):
+    # A choice whose logit is -inf or NaN has weight 0, whoever chose it.
+    torch = _torch()
+    logits = torch.zeros(3, 8)
+    logits[0, 2], logits[1, 2] = float("-inf"), float("nan")
+    ids = torch.tensor([[2, 5]] * 3, dtype=torch.int32, device="cuda")
+    out = []
+    for dw in (0.0, float("nan"), float("inf")):
+        dl = torch.empty(3, 8, device="cuda")
+        sg.sgemm_route_backward_tensors(logits.cuda(), ids, torch.tensor([[dw, 1.5]] * 3).cuda(), dl, renorm=renorm)
+        sg.check_status()
+        out.append(dl[:2])
+    assert torch.isfinite(out[0]).all()
+    assert torch.equal(out[0], out[1]) and torch.equal(out[0], out[2])
