@@ -57,14 +57,14 @@ class ExpertLayer:
         a = h.relu()
         y = torch.empty_like(rows)
         sg.sgemm_grouped_tensors(1.0, a, self.down, r["offsets"], 0.0, y, transw=True)
-        out = (y[r["place"]].float() * r["weights"][:, :, None]).sum(1).to(x.dtype)
+        out = (rows_of(y, r["place"]) * r["weights"][:, :, None]).sum(1).to(x.dtype)
         return out, (x, r, rows, h, a, y)
 
     def backward(self, dout, kept):
         """Gradients of x, router, up and down; the weights' in float32."""
         x, r, rows, h, a, y = kept
         off, order, place = r["offsets"], r["order"], r["place"]
-        dweights = (dout.float()[:, None, :] * y[place].float()).sum(-1)
+        dweights = (dout.float()[:, None, :] * rows_of(y, place)).sum(-1)
         dy = (dout.float()[order // self.top] * r["weights"].flatten()[order][:, None]).to(x.dtype)
         ddown = torch.empty(self.down.shape, device="cuda")
         sg.sgemm_grouped_wgrad_tensors(1.0, dy, a, off, 0.0, ddown)
@@ -77,7 +77,7 @@ class ExpertLayer:
         sg.sgemm_grouped_tensors(1.0, dh, self.up, off, 0.0, drows)
         dlogits = torch.empty_like(r["logits"])
         sg.sgemm_route_backward_tensors(r["logits"], r["experts"], dweights, dlogits)
-        dx = drows[place].float().sum(1)
+        dx = rows_of(drows, place).sum(1)
         sg.sgemm_tensors(1.0, dlogits, self.router, 1.0, dx)
         drouter = torch.empty_like(self.router)
         sg.sgemm_tensors(1.0, dlogits, x.float(), 0.0, drouter, transa=True)
@@ -100,6 +100,12 @@ class ExpertLayer:
         sg.sgemv_w4_tensors(h.relu(), q, s, y, self.group, zeros=z, experts=ids)
         y = y.view(x.shape[0], self.top, -1).float()
         return (y * r["weights"][:, :, None]).sum(1).to(x.dtype)
+
+
+def rows_of(y, place):
+    """The rows of y (rows, N) at place (tokens, top) in float32; zeros for a choice without an
+    expert (place -1), whose row no product wrote."""
+    return y[place].float().masked_fill((place < 0)[:, :, None], 0.0)
 
 
 def quantise(w, group):

@@ -88,3 +88,54 @@ def test_decode_is_the_layer_with_dequantised_weights():
     assert relative(got, ref) <= 4e-5
     # And the quantised layer is near the layer.
     assert relative(got, layer.forward(x)[0].double()) <= 0.3
+
+
+def test_masked_experts_leave_no_trace(monkeypatch):
+    # Tokens with fewer experts than choices, one with none: rows that no group
+    # writes are uninitialised (here NaN) and reach neither output nor gradient.
+    import torch
+    m = example()
+    layer = m.ExpertLayer(64, 96, 6, 3, dtype=torch.float32)
+    gen = torch.Generator().manual_seed(3)
+    masked = (torch.rand(50, 6, generator=gen) < 0.6).cuda()
+    masked[7] = True
+    masked[8] = False
+    route, empty, empty_like = sg.sgemm_route_tensors, torch.empty, torch.empty_like
+
+    def spoiled(t):
+        return t.fill_(float("nan")) if t.is_floating_point() else t
+
+    def masked_route(logits, *outputs):
+        logits.masked_fill_(masked[:logits.shape[0]], float("-inf"))
+        route(logits, *outputs)
+
+    with monkeypatch.context() as patch:
+        patch.setattr(torch, "empty", lambda *a, **k: spoiled(empty(*a, **k)))
+        patch.setattr(torch, "empty_like", lambda *a, **k: spoiled(empty_like(*a, **k)))
+        patch.setattr(m.sg, "sgemm_route_tensors", masked_route)
+        x = torch.randn(50, 64, device="cuda")
+        out, kept = layer.forward(x)
+        dout = torch.randn(50, 64, device="cuda")
+        grads = layer.backward(dout, kept)
+        layer.quantise(32)
+        few = layer.decode(x[:9])
+    sg.check_status()
+    leaves = [t.double().requires_grad_() for t in (x, layer.router, layer.up, layer.down)]
+    logits = (leaves[0] @ leaves[1].t()).masked_fill(masked, float("-inf"))
+    ref = torch.zeros_like(leaves[0])
+    experts = kept[1]["experts"]
+    assert bool((experts[7] < 0).all()) and bool((experts[8] >= 0).all())
+    for t in range(50):
+        ids = [e for e in experts[t].tolist() if e >= 0]
+        if not ids:
+            continue
+        weights = torch.softmax(logits[t, ids], 0)
+        row = sum(w * (torch.relu(leaves[0][t] @ leaves[2][e].t()) @ leaves[3][e].t())
+                  for w, e in zip(weights, ids))
+        ref = ref.index_add(0, torch.tensor([t], device="cuda"), row[None])
+    # As for the training step in float32 above.
+    assert torch.all(out[7] == 0) and relative(out, ref.detach()) <= 4e-5
+    ref.backward(dout.double())
+    for got, leaf in zip(grads, leaves):
+        assert relative(got, leaf.grad) <= 4e-5
+    assert torch.isfinite(few).all() and torch.all(few[7] == 0)
