@@ -15,7 +15,7 @@ from ._binding import (  # noqa: F401
     sgemm_host_tensors, sgemm_noalloc_check_status, sgemm_fp32_peak_ex, SGEMM_PEAK_FFMA,
     SGEMM_PEAK_FFMA2, SGEMM_PEAK_OUTER, sgemm_null_launch, sgemm_tf32_mma_peak, sgemm_selftest_occupy,
     sgemm_set_config, sgemm_set_shape_config, sgemm_clear_shape_configs, sgemm_set_wait_timeout_ns, sgemm_tensors, sgemm_3xtf32, sgemm_3xtf32_tensors,
-    SGEMM_TYPE_F32, SGEMM_TYPE_BF16, SGEMV_W4_MAX_K, sgemm_route, sgemm_route_backward, sgemm_grouped,
+    SGEMM_TYPE_F32, SGEMM_TYPE_BF16, SGEMV_W4_MAX_K, SGEMM_GROUPED_MAX_DIM, sgemm_route, sgemm_route_backward, sgemm_grouped,
     sgemm_grouped_wgrad, sgemv_w4, sgemm_route_tensors, sgemm_route_backward_tensors,
     sgemm_grouped_tensors, sgemm_grouped_wgrad_tensors, sgemv_w4_tensors,
 )

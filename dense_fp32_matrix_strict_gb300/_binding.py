@@ -38,6 +38,8 @@ SGEMM_OP_N, SGEMM_OP_T = 0, 1
 
 # Element types of the expert-layer entry points.
 SGEMM_TYPE_F32, SGEMM_TYPE_BF16 = 0, 1
+# Largest rows, M, N, K of the grouped products, and N of sgemv_w4.
+SGEMM_GROUPED_MAX_DIM = 2 ** 31 - 65536
 # Largest K of sgemv_w4.
 SGEMV_W4_MAX_K = 524288
 

@@ -17,7 +17,10 @@ namespace sg {
 // index read on the device was out of range; the kernel skipped it.
 constexpr int STATUS_BAD_INDEX = 32;
 
-constexpr int64_t kMaxDim = 0x7fffffff;
+constexpr int64_t kMaxDim = 0x7fffffff;              // of what only int64 arithmetic touches
+// Of sizes that the product kernels count in 32 bits. They step past a size by
+// a tile, or in the streaming kernel by a slab of at most 8192 k.
+constexpr int64_t kMaxGroupedDim = SGEMM_GROUPED_MAX_DIM;
 constexpr int64_t kMaxOffset = int64_t{1} << 59;     // elements; fits in int64 bytes
 constexpr int kMaxGroups = 1024;                     // experts of one call
 

@@ -328,8 +328,8 @@ int launch(int type, int out, bool wgrad, const Params& p, const DeviceInfo* dev
 }
 
 bool dims_ok(int64_t groups, int64_t rows, int64_t a, int64_t b) {
-    return groups >= 0 && groups <= kMaxGroups && rows >= 0 && rows <= kMaxDim && a >= 0 &&
-           a <= kMaxDim && b >= 0 && b <= kMaxDim;
+    return groups >= 0 && groups <= kMaxGroups && rows >= 0 && rows <= kMaxGroupedDim && a >= 0 &&
+           a <= kMaxGroupedDim && b >= 0 && b <= kMaxGroupedDim;
 }
 
 bool ld_ok(int64_t rows, int64_t cols, int64_t ld) {

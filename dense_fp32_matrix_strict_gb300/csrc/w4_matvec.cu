@@ -25,7 +25,7 @@ extern "C" int sgemv_w4(int type, int64_t pairs, int64_t repeat, int64_t N, int6
     using namespace sg::w4;
     if (type != SGEMM_TYPE_F32 && type != SGEMM_TYPE_BF16) return SGEMM_ERR_INVALID_VALUE;
     if (group != 32 && group != 64 && group != 128) return SGEMM_ERR_INVALID_VALUE;
-    if (pairs < 0 || N < 0 || K < 0 || pairs > 65535 || N > kMaxDim || K > SGEMV_W4_MAX_K ||
+    if (pairs < 0 || N < 0 || K < 0 || pairs > 65535 || N > kMaxGroupedDim || K > SGEMV_W4_MAX_K ||
         repeat < 1 || pairs % repeat != 0)
         return SGEMM_ERR_INVALID_VALUE;
     const int64_t bytes = (K + 1) / 2, groups = (K + group - 1) / group;

@@ -388,7 +388,8 @@ __global__ void __launch_bounds__(32 * WARPS, 1) w4_kernel(const X* __restrict__
         if (expert < 0 || expert >= p.num_experts) {
             if (expert >= p.num_experts && threadIdx.x == 0) atomicOr(p.status, STATUS_BAD_INDEX);
             // No expert: a row of zeros.
-            for (int n = blockIdx.x * THREADS + threadIdx.x; n < p.N; n += gridDim.x * THREADS) {
+            const int64_t step = static_cast<int64_t>(gridDim.x) * THREADS;
+            for (int64_t n = static_cast<int64_t>(blockIdx.x) * THREADS + threadIdx.x; n < p.N; n += step) {
                 if (p.ws != nullptr) p.ws[(blockIdx.z * p.pairs + pair0) * p.N + n] = 0.0f;
                 else store_f32(y + pair0 * p.ldy + n, 0.0f);
             }

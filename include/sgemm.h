@@ -499,6 +499,10 @@ SGEMM_API int sgemm_noalloc_check_status(cudaStream_t stream, int* bits);
 #define SGEMM_TYPE_F32 0    /* float; products by FP32 FMAs (strict, as sgemm)              */
 #define SGEMM_TYPE_BF16 1   /* bfloat16; results round once, to nearest even, when stored   */
 
+/* Largest size (rows, M, N, K; also N of sgemv_w4): the kernels count in 32
+ * bits and step past a size by up to a tile or a slab of a sum. */
+#define SGEMM_GROUPED_MAX_DIM 2147418112
+
 /*
  * sgemm_route — choose each token's experts and group the choices by expert.
  *
@@ -554,7 +558,7 @@ SGEMM_API int sgemm_route_backward(int type, int64_t T, int64_t E, int64_t top, 
  *   Y        rows x N of `type`, row stride ldy. Rows of no group are
  *            neither read nor written.
  *
- * 0 <= groups <= 1024, sizes up to 2^31 - 1, any strides and alignment of the
+ * 0 <= groups <= 1024, sizes up to SGEMM_GROUPED_MAX_DIM, any strides and alignment of the
  * element; Y may not overlap the inputs. beta == 0: Y is not read; alpha == 0
  * or K == 0: X and W are not read. FP32 runs FP32 FMAs, bfloat16 the tensor
  * cores; both accumulate in FP32. No row of one group is multiplied into
