@@ -114,11 +114,13 @@ __device__ __forceinline__ void fence_after() {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
 // Arrive on a barrier at a cluster address for a TMEM accumulator that has been
-// read. No write of this thread is handed over, so CTA scope will do: a
-// release at cluster scope would wait for the stores of the tile before
-// (265 us instead of 216, 32 experts of 256 rows, 4096 x 2048).
+// read. No write of this thread is handed over: what orders the reads before
+// the peer's next MMAs is the pair of tcgen05 fences around a relaxed arrival
+// of cluster scope and its wait. (A release at cluster scope would wait for the
+// stores of the tile before: 265 us instead of 216, 32 experts of 256 rows,
+// 4096 x 2048.)
 __device__ __forceinline__ void arrive_read(uint32_t cluster_addr) {
-    asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" :: "r"(cluster_addr)
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" :: "r"(cluster_addr)
                  : "memory");
 }
 // 32 consecutive FP32 columns of this thread's TMEM lane.
