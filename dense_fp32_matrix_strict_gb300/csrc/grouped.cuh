@@ -43,6 +43,11 @@ struct Params {
     int* status;
 };
 
+// A block that gives up a bounded wait stays until what it has in flight has
+// landed, however short the caller's limit is: this long without a barrier to
+// tell, thousands of times what a copy or an MMA takes.
+constexpr unsigned long long LAND_NS = 20000000ull;
+
 // Shared-memory schedule: off[0..groups], the groups by falling number of
 // rows (perm), and start[0..groups], the row tiles of at most `per` rows
 // before the group at each place of that order. A group whose offsets do not

@@ -155,8 +155,23 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
     for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// Bounded wait; on giving up sets the status bit and returns false. Acquires
-// at cluster scope (the peer's threads arrive on some of the barriers).
+// A thread of the pair gave up a wait. (Static: its address costs the main
+// loops no register.)
+__device__ __forceinline__ uint32_t* gave_up() {
+    __shared__ uint32_t word;
+    return &word;
+}
+
+// Bounded wait; on giving up sets the status bit and gave_up in both CTAs, and
+// returns false. Acquires at cluster scope (the peer's threads arrive on some
+// of the barriers).
+__device__ __forceinline__ void give_up(const Params& p, int code) {
+    atomicOr(p.status, code);
+#pragma unroll 1
+    for (uint32_t r = 0; r < 2; ++r)
+        asm volatile("st.relaxed.cluster.shared::cluster.u32 [%0], %1;"
+                     :: "r"(mapa_shared(smem_u32(gave_up()), r)), "r"(1u) : "memory");
+}
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, const Params& p, int code) {
     if (mbar_try_wait_cluster(bar, parity)) return true;
     const uint64_t t0 = globaltimer_ns();
@@ -165,10 +180,27 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, const Pa
         for (int i = 0; i < 16; ++i)
             if (mbar_try_wait_cluster(bar, parity)) return true;
         if (globaltimer_ns() - t0 > p.timeout_ns) {
-            atomicOr(p.status, code);
+            give_up(p, code);
             return false;
         }
     }
+}
+// The same for all lanes of a warp, which decide together: what follows is
+// warp-collective, and one lane's clock may pass the limit where another's
+// does not.
+__device__ __forceinline__ bool warp_wait_bar(uint32_t bar, uint32_t parity, const Params& p, int code) {
+    bool done = mbar_try_wait_cluster(bar, parity);
+    if (__all_sync(0xffffffffu, done)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    do {
+#pragma unroll 1
+        for (int i = 0; i < 16; ++i) {
+            done = done || mbar_try_wait_cluster(bar, parity);
+            if (__all_sync(0xffffffffu, done)) return true;
+        }
+    } while (__all_sync(0xffffffffu, globaltimer_ns() - t0 <= p.timeout_ns));
+    if ((threadIdx.x & 31) == 0) give_up(p, code);
+    return false;
 }
 
 // One output tile. Forward: group g, rows row0 .. row0 + valid (at most 256),
@@ -300,6 +332,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             mbar_init(acce0 + 8 * b, 2 * EPI_WARPS);      // both CTAs' epilogue warps (rank 0's)
         }
         mbar_init(done_bar, 1);
+        *gave_up() = 0;
         fence_barrier_init();
     }
     if (warp == 1) {
@@ -384,8 +417,6 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                     if (++s == STAGES) { s = 0; ph ^= 1u; }
                 }
             }
-            // A producer that gives up has waited the whole time limit for a
-            // stage, far longer than any copy it issued takes to land.
         }
     } else if (warp == 1) {
         if (leader && lane == 0) {
@@ -415,8 +446,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                             break;
                         }
                         if (WGRAD && (kb + 1) * BK > it.depth) {
-                            if (!wait_bar(clean0 + 8 * s, (cleaned >> s) & 1u, p,
-                                          STATUS_CONSUMER_TIMEOUT)) {
+                            if (!wait_bar(clean0 + 8 * s, (cleaned >> s) & 1u, p, STATUS_CONSUMER_TIMEOUT)) {
                                 ok = false;
                                 break;
                             }
@@ -481,12 +511,11 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                 for (int j = 0; j < SPAN; ++j) acc[j] = 0.0f;
                 for (int c = 0; c < parts; ++c, ++n) {
                     const int b = n & 1;
-                    if (!wait_bar(accf0 + 8 * b, static_cast<uint32_t>((n >> 1) & 1), p,
-                                  STATUS_CONSUMER_TIMEOUT)) {
+                    if (!warp_wait_bar(accf0 + 8 * b, static_cast<uint32_t>((n >> 1) & 1), p,
+                                       STATUS_CONSUMER_TIMEOUT)) {
                         ok = false;
                         break;
                     }
-                    __syncwarp();
                     fence_after();
 #pragma unroll
                     for (int ch = 0; ch < SPAN; ch += 16) {
@@ -506,11 +535,10 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             } else {
                 const int b = n & 1;
                 if (parts > 0) {
-                    if (!wait_bar(accf0 + 8 * b, static_cast<uint32_t>((n >> 1) & 1), p,
-                                  STATUS_CONSUMER_TIMEOUT))
+                    if (!warp_wait_bar(accf0 + 8 * b, static_cast<uint32_t>((n >> 1) & 1), p,
+                                       STATUS_CONSUMER_TIMEOUT))
                         break;
                     ++n;
-                    __syncwarp();                   // tcgen05.ld is warp-collective
                     fence_after();
                 }
                 for (int ch = 0; ch < SPAN && c0 + ch < it.width; ch += 32) {
@@ -536,7 +564,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             s = (s + it.ke - it.kb - 1) % STAGES;
             const int left = it.depth - (it.ke - 1) * BK;
             if (left < BK) {
-                if (!wait_bar(land0 + 8 * s, (phases >> s) & 1u, p, STATUS_CONSUMER_TIMEOUT)) break;
+                if (!warp_wait_bar(land0 + 8 * s, (phases >> s) & 1u, p, STATUS_CONSUMER_TIMEOUT)) break;
                 phases ^= 1u << s;
                 // Four boxes of 64 k rows of 128 bytes; a k row stays one
                 // 128-byte line under the swizzle.
@@ -559,10 +587,17 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     // Single exit: every role is done (or gave up after its bounded waits);
     // rank 0's MMA thread has seen its last MMA finish, and the cluster
     // barrier makes the peer wait for that before the TMEM of both is freed.
+    // If a wait was given up, no barrier vouches for the copies and MMAs of
+    // either CTA (rank 1's bytes complete on rank 0's barriers, and one
+    // producer may be stages ahead of the other): both CTAs stay LAND_NS.
     fence_before();
     __syncthreads();
     cluster_sync();
     fence_after();
+    if (*static_cast<volatile uint32_t*>(gave_up()) != 0) {
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < LAND_NS) __nanosleep(1000);
+    }
     if (warp == 1) {
         __syncwarp();
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;"
