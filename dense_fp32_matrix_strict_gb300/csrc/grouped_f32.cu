@@ -91,18 +91,22 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* desc, uint
         : "memory");
 }
 
-__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, const Params& p, int code) {
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, unsigned long long limit,
+                                         const Params& p, int code) {
     if (mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = globaltimer_ns();
     for (;;) {
 #pragma unroll 1
         for (int i = 0; i < 16; ++i)
             if (mbar_try_wait(bar, parity)) return true;
-        if (globaltimer_ns() - t0 > p.timeout_ns) {
+        if (globaltimer_ns() - t0 > limit) {
             atomicOr(p.status, code);
             return false;
         }
     }
+}
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, const Params& p, int code) {
+    return wait_for(bar, parity, p.timeout_ns, p, code);
 }
 
 // An output tile: rows row0 .. row0 + valid of Y (forward) or mrow .. of D
@@ -260,12 +264,13 @@ tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                 if (++s == STAGES) { s = 0; ph ^= 1u; }
             }
         }
-        if (!ok) {
-            // Let this thread's copies land before the CTA can exit.
+        // The copies land before the block can end, whoever gave up waiting
+        // (the consumers may have gone) and however short the limit is.
+        if (t == 0) {
             const int n = issued < STAGES ? issued : STAGES;
             for (int j = 0; j < n; ++j) {
                 if (--s < 0) { s = STAGES - 1; ph ^= 1u; }
-                wait_bar(full0 + 8 * s, ph, p, STATUS_DRAIN_TIMEOUT);
+                wait_for(full0 + 8 * s, ph, max(p.timeout_ns, LAND_NS), p, STATUS_DRAIN_TIMEOUT);
             }
         }
         return;
