@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(256) simple_kernel(const Params p) {
             for (int j = 0; j < 4; ++j) {
                 const int n = j0 + 4 * tx + j;
                 if (n >= p.N) continue;
-                float v = p.alpha * acc[i][j];
+                float v = depth > 0 ? p.alpha * acc[i][j] : 0.0f;   // (empty: whatever alpha is)
                 if (p.beta != 0.0f) v = fmaf(p.beta, load_f32(out + n), v);
                 store_f32(out + n, v);
             }

@@ -490,17 +490,19 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                 const int col = it.col + in_tile;
                 const int rows = col < p.N ? it.valid - c0 - ch : 0;
                 const bool cut = piece.slot >= 0;
+                // (An empty sum is zero whatever alpha is.)
+                const float alpha = WGRAD && it.depth == 0 ? 0.0f : p.alpha;
                 float* slot = p.tail_ws + static_cast<int64_t>(piece.slot) * TILE * TILE +
                               (c0 + ch) * TILE + in_tile;
                 O* out = static_cast<O*>(p.y) + (col < p.N ? col : 0) + (c0 + ch) * p.ldy +
                          (WGRAD ? it.g * p.stride_y + it.ncol * p.ldy : it.row0 * p.ldy);
                 if constexpr (sizeof(O) == 4) {
                     write_rows(cut ? slot : reinterpret_cast<float*>(out), cut ? TILE : p.ldy,
-                               cut ? 1.0f : p.alpha, cut ? 0.0f : p.beta, rows, v);
+                               cut ? 1.0f : alpha, cut ? 0.0f : p.beta, rows, v);
                 } else if (cut) {
                     write_rows(slot, TILE, 1.0f, 0.0f, rows, v);
                 } else {
-                    write_rows(out, p.ldy, p.alpha, p.beta, rows, v);
+                    write_rows(out, p.ldy, alpha, p.beta, rows, v);
                 }
             };
             const int parts = part_count<WGRAD>(it);

@@ -398,7 +398,9 @@ tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         // Outputs: alpha * sum + beta * y, or a piece's sums to a slot of BM x BN.
         const bool cut = piece.slot >= 0;
         const int64_t ld = cut ? BN : p.ldy;
-        const float alpha = cut ? 1.0f : p.alpha, beta = cut ? 0.0f : p.beta;
+        // (An empty sum is zero whatever alpha is.)
+        const float alpha = cut ? 1.0f : MODE == WGRAD && it.depth == 0 ? 0.0f : p.alpha;
+        const float beta = cut ? 0.0f : p.beta;
         const int cols = cut ? BN : p.N - it.col;
         const bool vec = (cut || p.y_vec) && beta == 0.0f && cols >= BN;
         float* base = cut ? p.tail_ws + static_cast<int64_t>(piece.slot) * BM * BN

@@ -345,3 +345,26 @@ def test_same_bits_on_every_call_and_another_stream(dtype):
             got.append((y, d))
         for y, d in got[1:]:
             assert torch.equal(y, got[0][0]) and torch.equal(d, got[0][1])
+
+
+@pytest.mark.parametrize("dtype,out", WGRAD)
+@pytest.mark.parametrize("alpha", [float("inf"), float("nan"), -3e38])
+@pytest.mark.parametrize("beta", [0.0, -2.0])
+def test_alpha_has_no_part_in_empty_sums(dtype, out, alpha, beta):
+    # A group without rows gets beta * D, and K = 0 beta * Y, whatever alpha is.
+    torch = _torch()
+    dt, ot = getattr(torch, dtype), getattr(torch, out)
+    for sizes in ([70, 0, 5, 0], [0, 0], [0, 4001]):
+        p, q = torch.ones(sum(sizes), 70, device="cuda").to(dt), torch.ones(sum(sizes), 136, device="cuda").to(dt)
+        d0 = torch.randn(len(sizes), 70, 136, device="cuda").to(ot)
+        d = d0.clone() if beta else torch.full_like(d0, float("nan"))
+        sg.sgemm_grouped_wgrad_tensors(alpha, p, q, offsets_of(sizes), beta, d)
+        sg.check_status()
+        for e, n in enumerate(sizes):
+            if n == 0:
+                assert torch.equal(d[e], (beta * d0[e].float()).to(ot) if beta else torch.zeros_like(d[e]))
+    y0 = torch.randn(9, 40, device="cuda").to(dt)
+    y = y0.clone() if beta else torch.full_like(y0, float("nan"))
+    sg.sgemm_grouped_tensors(alpha, y0[:, :0], torch.empty(2, 0, 40, device="cuda", dtype=dt), offsets_of([4, 5]), beta, y)
+    sg.check_status()
+    assert torch.equal(y, (beta * y0.float()).to(dt) if beta else torch.zeros_like(y))
