@@ -1,5 +1,5 @@
 // grouped.cu — matrix products grouped by expert with ragged sizes: the entry
-// points, and a kernel that takes every layout.
+// points, the choice of a kernel, and the small kernels beside the products.
 //
 //   forward / input gradient:  Y[r] = alpha * X[r] op(W_g) + beta * Y[r]
 //   weight gradient:           D_g = alpha * P_g^T Q_g + beta * D_g
@@ -14,96 +14,41 @@
 namespace sg {
 namespace grouped {
 
-// 64 x 64 tiles, 16 k at a time through shared memory, 4 x 4 outputs per
-// thread in FP32 FMAs. Element strides describe the operands, so any base,
-// leading dimension and orientation is taken.
-constexpr int ST = 64, SK = 16;
+// Calls without a sum (alpha == 0, K == 0, no rows at all): beta times the rows
+// of Y that belong to a group, or times every D_g. 32 rows x 256 columns per
+// item, neighbouring threads on neighbouring columns; bound by its bytes.
+constexpr int SCALE_ROWS = 32, SCALE_COLS = 256;
 
-template <typename T, typename O, bool WGRAD>
-__global__ void __launch_bounds__(256) simple_kernel(const Params p) {
+template <typename O, bool WGRAD>
+__global__ void __launch_bounds__(SCALE_COLS) scale_kernel(const Params p) {
     extern __shared__ int sched_sm[];
-    __shared__ float as[SK][ST + 4], bs[SK][ST + 4];
-    const Schedule sch = build_schedule(p, ST, sched_sm);
-    const T* x = static_cast<const T*>(p.x);
-    const T* w = static_cast<const T*>(p.w);
-    O* y = static_cast<O*>(p.y);
-    const int tiles_n = (p.N + ST - 1) / ST;
-    const int tiles_m = (p.K + ST - 1) / ST;            // weight gradient: K is M
-    const int64_t items = WGRAD ? static_cast<int64_t>(p.groups) * tiles_m * tiles_n
-                                : static_cast<int64_t>(sch.start[p.groups]) * tiles_n;
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    const Schedule sch = build_schedule(p, SCALE_ROWS, sched_sm);
+    const int strips = (p.N + SCALE_COLS - 1) / SCALE_COLS;
+    const int tiles_m = (p.K + SCALE_ROWS - 1) / SCALE_ROWS;      // weight gradient: K is M
+    const int64_t items =
+        strips * (WGRAD ? static_cast<int64_t>(p.groups) * tiles_m : static_cast<int64_t>(sch.start[p.groups]));
     for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-        int g, i0, depth;
-        int64_t row0, row_end;
-        const int j0 = static_cast<int>(item % tiles_n) * ST;
+        const int64_t t = item / strips;
+        const int n = static_cast<int>(item - t * strips) * SCALE_COLS + threadIdx.x;
+        if (n >= p.N) continue;
+        int64_t row, end;
+        O* y = static_cast<O*>(p.y) + n;
         if (WGRAD) {
-            const int64_t m = item / tiles_n;
-            g = static_cast<int>(m / tiles_m);
-            i0 = static_cast<int>(m % tiles_m) * ST;
-            row0 = sch.off[g];
-            // Empty, refused, or alpha == 0.
-            row_end = p.x == nullptr ? row0 : row0 + max(0, group_rows(sch, p.rows, g));
-            depth = static_cast<int>(row_end - row0);
+            const int64_t g = t / tiles_m;
+            y += g * p.stride_y;
+            row = (t - g * tiles_m) * SCALE_ROWS;
+            end = p.K;
         } else {
-            const int t = static_cast<int>(item / tiles_n);
-            const int place = place_of(sch, p.groups, t);
-            g = sch.perm[place];
-            i0 = 0;
-            row0 = sch.off[g] + static_cast<int64_t>(t - sch.start[place]) * ST;
-            row_end = sch.off[g + 1];
-            depth = p.K;
+            const int place = place_of(sch, p.groups, static_cast<int>(t));
+            const int g = sch.perm[place];
+            row = sch.off[g] + (t - sch.start[place]) * SCALE_ROWS;
+            end = sch.off[g + 1];
         }
-        const T* wg = WGRAD ? w : w + g * p.stride_w;
-        float acc[4][4] = {};
-        for (int k0 = 0; k0 < depth; k0 += SK) {
-            for (int e = threadIdx.x; e < ST * SK; e += 256) {
-                float a = 0.0f, b = 0.0f;
-                if (WGRAD) {
-                    const int i = e % ST, k = e / ST;
-                    if (k0 + k < depth) {
-                        if (i0 + i < p.K) a = load_f32(x + (row0 + k0 + k) * p.ldx + i0 + i);
-                        if (j0 + i < p.N) b = load_f32(w + (row0 + k0 + k) * p.ldw + j0 + i);
-                    }
-                    as[k][i] = a;
-                    bs[k][i] = b;
-                } else {
-                    const int k = e % SK, i = e / SK;
-                    if (k0 + k < depth && row0 + i < row_end)
-                        a = load_f32(x + (row0 + i) * p.ldx + k0 + k);
-                    as[k][i] = a;
-                    const int kb = p.opw ? k : e / ST, jb = p.opw ? i : e % ST;
-                    if (k0 + kb < depth && j0 + jb < p.N)
-                        b = load_f32(p.opw ? wg + (j0 + jb) * p.ldw + k0 + kb
-                                           : wg + (k0 + kb) * p.ldw + j0 + jb);
-                    bs[kb][jb] = b;
-                }
-            }
-            __syncthreads();
-#pragma unroll
-            for (int k = 0; k < SK; ++k) {
-                const float4 a = *reinterpret_cast<const float4*>(&as[k][4 * ty]);
-                const float4 b = *reinterpret_cast<const float4*>(&bs[k][4 * tx]);
-                const float av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(av[i], bv[j], acc[i][j]);
-            }
-            __syncthreads();
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t r = WGRAD ? i0 + 4 * ty + i : row0 + 4 * ty + i;
-            if (r >= (WGRAD ? static_cast<int64_t>(p.K) : row_end)) continue;
-            O* out = y + (WGRAD ? g * p.stride_y : 0) + r * p.ldy;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int n = j0 + 4 * tx + j;
-                if (n >= p.N) continue;
-                float v = depth > 0 ? p.alpha * acc[i][j] : 0.0f;   // (empty: whatever alpha is)
-                if (p.beta != 0.0f) v = fmaf(p.beta, load_f32(out + n), v);
-                store_f32(out + n, v);
-            }
+        end = min(end, row + SCALE_ROWS);
+#pragma unroll 4
+        for (; row < end; ++row) {
+            O* o = y + row * p.ldy;
+            store_f32(o, p.beta != 0.0f ? fmaf(p.beta, load_f32(o), 0.0f) : 0.0f);
         }
     }
 }
@@ -137,16 +82,6 @@ __global__ void __launch_bounds__(256) pack_kernel(const T* __restrict__ src, in
         }
     }
     griddep_wait();
-}
-
-using SimpleKernel = void (*)(Params);
-
-SimpleKernel simple_for(int type, int out, bool wgrad) {
-    if (type == SGEMM_TYPE_F32)
-        return wgrad ? &simple_kernel<float, float, true> : &simple_kernel<float, float, false>;
-    if (!wgrad) return &simple_kernel<__nv_bfloat16, __nv_bfloat16, false>;
-    return out == SGEMM_TYPE_BF16 ? &simple_kernel<__nv_bfloat16, __nv_bfloat16, true>
-                                  : &simple_kernel<__nv_bfloat16, float, true>;
 }
 
 // One operand that TMA cannot read in place: rows x cols, mats of them.
@@ -262,61 +197,66 @@ cudaError_t run_skinny(Params p, const DeviceInfo* dev, cudaMemPool_t pool, cuda
     return e;
 }
 
+// Copies that the product cannot do without and slots that it can: without
+// memory for the copies the call fails, without slots the last round stays
+// uncut.
 cudaError_t run(int type, int out, bool wgrad, Params p, const DeviceInfo* dev, cudaMemPool_t pool,
                 cudaStream_t stream) {
     const bool half = type == SGEMM_TYPE_BF16;
-    const bool reads = p.K > 0 && p.rows > 0 && p.x != nullptr;
     const int64_t vec = half ? 8 : 4;
     p.y_vec = ptr_aligned(p.y, 16) && p.ldy % 4 == 0 && p.stride_y % 4 == 0;
     p.parts = 1;
     p.part_stride = 0;
     p.tail_ws = nullptr;
     p.pdl = 0;
-    if (reads) {
-        if (!wgrad && !half && p.rows <= p.groups * skinny_rows(p.opw)) return run_skinny(p, dev, pool, stream);
-        const Packed kx = plan_pack(p.x, p.rows, p.K, 1, p.ldx, 0, vec);
-        Packed kw = wgrad ? plan_pack(p.w, p.rows, p.N, 1, p.ldw, 0, vec)
-                          : plan_pack(p.w, p.opw ? p.N : p.K, p.opw ? p.K : p.N, p.groups, p.ldw,
-                                      p.stride_w, vec);
-        p.w_tma = !kw.on;
-        if (!wgrad && !half) {
-            kw.on = false;                             // read in place
-            kw.bytes = 0;
-        }
-        const Tail t = half ? bf16_tail(p, wgrad, dev) : f32_tail(p, wgrad, dev);
-        const bool cut = t.items < kCutRounds * t.workers && t.blocks >= t.worth;
-        const size_t slots = cut ? 2 * static_cast<size_t>(t.workers) * t.slot_bytes : 0;
-        void* ws = nullptr;
-        const size_t bytes = kx.bytes + kw.bytes + slots;
-        if (bytes == 0 || cudaMallocFromPoolAsync(&ws, bytes, pool, stream) == cudaSuccess) {
-            unsigned char* at = static_cast<unsigned char*>(ws);
-            cudaError_t e = cudaSuccess;
-            if (kx.on) {
-                e = pack(type, kx, p.x, p.ldx, 0, at, nullptr, dev, stream, false);
-                p.x = at;
-                p.ldx = kx.ld;
-            }
-            if (kw.on && e == cudaSuccess) {
-                void* w2 = at + kx.bytes;
-                e = pack(type, kw, p.w, p.ldw, p.stride_w, w2, wgrad ? nullptr : p.offsets, dev, stream,
-                         kx.on && pdl_enabled());
-                p.w = w2;
-                p.ldw = kw.ld;
-                p.stride_w = kw.rows * kw.ld;
-            }
-            p.pdl = (kx.on || kw.on) && pdl_enabled();
-            if (cut) p.tail_ws = reinterpret_cast<float*>(at + kx.bytes + kw.bytes);
-            if (e == cudaSuccess)
-                e = half ? launch_bf16(p, wgrad, dev, stream) : launch_f32(p, wgrad, dev, stream);
-            if (ws != nullptr) cudaFreeAsync(ws, stream);
-            return e;
-        }
-        // No workspace: the kernel that takes any layout.
-        (void)cudaGetLastError();
+    if (p.K == 0 || p.rows == 0 || p.x == nullptr) {
+        void (*const scale)(Params) =
+            wgrad ? (out == SGEMM_TYPE_BF16 ? &scale_kernel<__nv_bfloat16, true> : &scale_kernel<float, true>)
+                  : (half ? &scale_kernel<__nv_bfloat16, false> : &scale_kernel<float, false>);
+        return launch_kernel(scale, dim3(4 * dev->sm_count), dim3(SCALE_COLS),
+                             schedule_ints(p.groups) * sizeof(int), stream, false, 1, p);
     }
-    const size_t smem = schedule_ints(p.groups) * sizeof(int);
-    return launch_kernel(simple_for(type, out, wgrad), dim3(4 * dev->sm_count), dim3(256), smem, stream,
-                         false, 1, p);
+    if (!wgrad && !half && p.rows <= p.groups * skinny_rows(p.opw)) return run_skinny(p, dev, pool, stream);
+    const Packed kx = plan_pack(p.x, p.rows, p.K, 1, p.ldx, 0, vec);
+    Packed kw = wgrad ? plan_pack(p.w, p.rows, p.N, 1, p.ldw, 0, vec)
+                      : plan_pack(p.w, p.opw ? p.N : p.K, p.opw ? p.K : p.N, p.groups, p.ldw,
+                                  p.stride_w, vec);
+    p.w_tma = !kw.on;
+    if (!wgrad && !half) {
+        kw.on = false;                                 // read in place
+        kw.bytes = 0;
+    }
+    const Tail t = half ? bf16_tail(p, wgrad, dev) : f32_tail(p, wgrad, dev);
+    bool cut = t.items < kCutRounds * t.workers && t.blocks >= t.worth;
+    const size_t copies = kx.bytes + kw.bytes, slots = 2 * static_cast<size_t>(t.workers) * t.slot_bytes;
+    void* ws = nullptr;
+    cudaError_t e = cudaSuccess;
+    if (cut && cudaMallocFromPoolAsync(&ws, copies + slots, pool, stream) != cudaSuccess) {
+        (void)cudaGetLastError();
+        cut = false;
+    }
+    if (!cut && copies > 0) e = cudaMallocFromPoolAsync(&ws, copies, pool, stream);
+    if (e != cudaSuccess) return e;
+    unsigned char* at = static_cast<unsigned char*>(ws);
+    if (kx.on) {
+        e = pack(type, kx, p.x, p.ldx, 0, at, nullptr, dev, stream, false);
+        p.x = at;
+        p.ldx = kx.ld;
+    }
+    if (kw.on && e == cudaSuccess) {
+        void* w2 = at + kx.bytes;
+        e = pack(type, kw, p.w, p.ldw, p.stride_w, w2, wgrad ? nullptr : p.offsets, dev, stream,
+                 kx.on && pdl_enabled());
+        p.w = w2;
+        p.ldw = kw.ld;
+        p.stride_w = kw.rows * kw.ld;
+    }
+    p.pdl = (kx.on || kw.on) && pdl_enabled();
+    if (cut) p.tail_ws = reinterpret_cast<float*>(at + copies);
+    if (e == cudaSuccess)
+        e = half ? launch_bf16(p, wgrad, dev, stream) : launch_f32(p, wgrad, dev, stream);
+    if (ws != nullptr) cudaFreeAsync(ws, stream);
+    return e;
 }
 
 int launch(int type, int out, bool wgrad, const Params& p, const DeviceInfo* dev, cudaMemPool_t pool,
@@ -324,7 +264,7 @@ int launch(int type, int out, bool wgrad, const Params& p, const DeviceInfo* dev
     const cudaError_t e = run(type, out, wgrad, p, dev, pool, stream);
     if (e == cudaSuccess) return SGEMM_OK;
     (void)cudaGetLastError();
-    return cuda_fail(e, SGEMM_ERR_LAUNCH);
+    return cuda_fail(e, e == cudaErrorMemoryAllocation ? SGEMM_ERR_CUDA : SGEMM_ERR_LAUNCH);
 }
 
 bool dims_ok(int64_t groups, int64_t rows, int64_t a, int64_t b) {

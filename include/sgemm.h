@@ -493,6 +493,21 @@ SGEMM_API int sgemm_noalloc_check_status(cudaStream_t stream, int* bits);
  * number of experts counts as none; either sets status bit 32, and
  * sgemm_check_status returns SGEMM_ERR_DEVICE_CHECK. Groups must not share
  * rows (offsets increase), else the shared rows' results are undefined.
+ *
+ * Workspaces come from the library's stream-ordered pool, as above. The grouped
+ * products take:
+ *   - aligned copies (rows padded to 16 bytes) of operands whose base, row or
+ *     matrix stride is not a multiple of 16 bytes: X, P and Q whole, bfloat16 W
+ *     for all groups. A float W, and X where float groups have few rows, are
+ *     read in place;
+ *   - where the last round of tiles is cut along k, two slots of sums per
+ *     worker: at most 512 KB for each pair of SMs (bfloat16), 128 KB for each
+ *     SM (float);
+ *   - where float groups have few rows and their sums are split, up to 32 times
+ *     rows x N floats.
+ * A call that gets no memory for a copy returns SGEMM_ERR_CUDA and runs
+ * nothing; the last two are done without. sgemm_route and sgemv_w4 return
+ * SGEMM_ERR_CUDA where theirs (below) cannot be had.
  */
 
 /* Element types. Products accumulate in FP32 whatever the type. */
@@ -522,8 +537,8 @@ SGEMM_API int sgemm_noalloc_check_status(cudaStream_t stream, int* bits);
  *
  * 1 <= top <= min(32, E), 1 <= E <= 1024, T * top < 2^31. The same result on
  * every call (no order of atomics shows). Up to 256 tokens take one kernel,
- * more take two and a workspace of at most 4 * SMs * E bytes from the
- * library's pool. Outputs may not overlap the logits or one another.
+ * more take two and a workspace of at most 4 * SMs * E bytes (E rounded up
+ * to a multiple of 4) from the library's pool. Outputs may not overlap the logits or one another.
  */
 SGEMM_API int sgemm_route(int type, int64_t T, int64_t E, int64_t top, int renorm,
                           const void* logits, int64_t ldl, float* weights, int32_t* experts,
@@ -611,7 +626,8 @@ SGEMM_API int sgemm_grouped_wgrad(int type, int64_t groups, int64_t rows, int64_
  * The sum over a group is formed from exact products in FP32 and scaled once.
  * 0 <= K <= SGEMV_W4_MAX_K; rows of Q on 16-byte boundaries (Q, ldq,
  * stride_q) load fastest. Long K of many tokens is taken in slabs whose sums
- * a second kernel joins, through a workspace from the library's pool.
+ * a second kernel joins, through a workspace of slabs * pairs * N floats from
+ * the library's pool.
  */
 SGEMM_API int sgemv_w4(int type, int64_t pairs, int64_t repeat, int64_t N, int64_t K,
                        int64_t group, const void* X, int64_t ldx, const uint8_t* Q, int64_t ldq,

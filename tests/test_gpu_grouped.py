@@ -368,3 +368,26 @@ def test_alpha_has_no_part_in_empty_sums(dtype, out, alpha, beta):
     sg.sgemm_grouped_tensors(alpha, y0[:, :0], torch.empty(2, 0, 40, device="cuda", dtype=dt), offsets_of([4, 5]), beta, y)
     sg.check_status()
     assert torch.equal(y, (beta * y0.float()).to(dt) if beta else torch.zeros_like(y))
+
+
+def test_a_copy_without_memory_is_an_error():
+    # Rows of one bfloat16 each, copied to rows of 16 bytes: eight times what the
+    # weights take (51 GB), more than the GPU has. The call says so; nothing ran.
+    torch = _torch()
+    N, E = sg.SGEMM_GROUPED_MAX_DIM, 12
+    w = torch.empty(E, N, 1, device="cuda", dtype=torch.bfloat16)
+    x = torch.ones(1, 1, device="cuda", dtype=torch.bfloat16)
+    y = torch.empty(1, N, device="cuda", dtype=torch.bfloat16)
+    y[0, :1000] = 3.0
+    off = torch.tensor([0] + [1] * E, dtype=torch.int32, device="cuda")
+    assert E * N * 16 > torch.cuda.get_device_properties(0).total_memory
+    try:
+        with pytest.raises(sg.SgemmError) as error:
+            sg.sgemm_grouped_tensors(1.0, x, w, off, 0.0, y, transw=True)
+        assert error.value.code == sg.SGEMM_ERR_CUDA
+        sg.check_status()
+        assert torch.all(y[0, :1000] == 3.0)
+    finally:
+        del w, y
+        torch.cuda.empty_cache()
+    forward([70, 0, 200, 3], 131, 77, torch.bfloat16, True)
