@@ -667,7 +667,8 @@ def sgemv_w4_tensors(X, Q, scales, Y, group, zeros=None, experts=None, stream=No
 
     X (tokens, K) and Y (pairs, N), float32 or bfloat16, pairs = repeat *
     tokens; Q (N, ceil(K / 2)) uint8, the lower half of a byte first; scales
-    (N, ceil(K / group)) of X's type and zeros the same shape in uint8 (None: 8).
+    (N, ceil(K / group)) of X's type and zeros the same shape in uint8, any
+    value (None: 8).
     With experts (pairs,) int32 on the device, Q, scales and zeros have a
     leading dimension of experts and row p uses those of experts[p] (negative:
     a row of zeros).

@@ -129,7 +129,8 @@ __device__ __forceinline__ uint32_t unpack_pair(uint32_t bits, uint32_t mul, uin
     asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(v) : "r"(bits), "r"(mul), "r"(off));
     return v;
 }
-// -z * 2^-6 as two BF16 numbers, z < 128: its bits are z * 2^-133.
+// -z * 2^-6 as two BF16 numbers, for any byte: its bits are z * 2^-133, from
+// z = 128 on in the first binade, and q - z stays within 8 bits.
 __device__ __forceinline__ uint32_t zero_pair(uint32_t z) {
     return unpack_pair(z * 0x00010001u, 0xff00ff00u, 0x80008000u);
 }

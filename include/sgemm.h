@@ -617,7 +617,7 @@ SGEMM_API int sgemm_grouped_wgrad(int type, int64_t groups, int64_t rows, int64_
  *            q[2i] in its low and q[2i + 1] in its high half. With experts,
  *            stride_q bytes between experts.
  *   scales   N x ceil(K / group) of `type`, contiguous (per expert).
- *   zeros    the same shape in bytes, each 0 to 127, or NULL for 8.
+ *   zeros    the same shape in bytes, any value of a byte, or NULL for 8.
  *   group    32, 64 or 128.
  *   experts  pairs int32 on the device, or NULL. A negative index means no
  *            expert: the row of Y is zeros.

@@ -284,3 +284,18 @@ def test_host_threads_call_concurrently(tmp_path):
     torch.cuda.synchronize()
     for x, q, s, y, stream, want in kept:
         assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_every_code_with_every_zero_point(group, dtype):
+    # q - z for all 16 codes and 256 zero points: integers below 2^8, which the
+    # unpacking and the sum of a one-input token keep exactly.
+    torch = _torch()
+    dtype = getattr(torch, dtype)
+    N, K = 256, 16
+    x = torch.eye(K).to(dtype)
+    q = torch.tensor([2 * i | (2 * i + 1) << 4 for i in range(8)], dtype=torch.uint8).repeat(N, 1)
+    z = torch.arange(N, dtype=torch.uint8).view(N, 1)
+    y = call(x, q, torch.ones(N, 1, dtype=dtype), z, group, K, N)
+    assert torch.equal(y.cpu().float(), torch.arange(K).view(K, 1).float() - torch.arange(N).float())
