@@ -139,3 +139,45 @@ def test_masked_experts_leave_no_trace(monkeypatch):
     for got, leaf in zip(grads, leaves):
         assert relative(got, leaf.grad) <= 4e-5
     assert torch.isfinite(few).all() and torch.all(few[7] == 0)
+
+
+def test_host_threads_train_concurrently():
+    # Each thread runs steps of its own sizes and type on its own stream; all
+    # get the bits of a run by themselves.
+    import threading
+
+    import torch
+    m = example()
+    shapes = [(50, 64, 96, 6, 2, torch.float32), (300, 100, 37, 16, 4, torch.bfloat16),
+              (700, 256, 384, 8, 2, torch.bfloat16), (20, 512, 256, 12, 3, torch.float32)]
+    cases = []
+    for i, (tokens, hidden, inner, experts, top, dtype) in enumerate(shapes):
+        layer = m.ExpertLayer(hidden, inner, experts, top, dtype=dtype, seed=i)
+        x = torch.randn(tokens, hidden, device="cuda").to(dtype)
+
+        def step(layer=layer, x=x):
+            out, kept = layer.forward(x)
+            return (out, *layer.backward(torch.ones_like(out), kept))
+
+        cases.append((step, [t.clone() for t in step()], torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    failed, start = [], threading.Barrier(len(cases))
+
+    def work(step, want, stream):
+        try:
+            start.wait()
+            with torch.cuda.stream(stream):
+                for _ in range(20):
+                    got = step()
+                stream.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+        except Exception as e:                  # reported below, on the main thread
+            failed.append(repr(e))
+
+    threads = [threading.Thread(target=work, args=c) for c in cases]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
+    sg.check_status()
