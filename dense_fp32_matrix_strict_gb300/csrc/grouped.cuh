@@ -8,6 +8,16 @@
 namespace sg {
 namespace grouped {
 
+// When the last round of tiles is cut: whole it lasts as long as its longest
+// sum, cut it lasts a worker's share, and what that saves, in blocks of k, has
+// to reach the price of slots and joining. The price grows with the part r of
+// the workers that have a whole tile (the rest of the GPU's bandwidth is idle
+// then, and a tile alone is faster): base + slope * r up to a half, above that
+// `over`.
+struct TailRule {
+    int base, slope, over;
+};
+
 // What every grouped kernel takes. Forward (and input gradient): output rows
 // off[g] .. off[g+1] are X's rows times W_g (opw: 0 stored K x N, 1 stored
 // N x K). Weight gradient: D_g (M x N) = P^T Q over those rows; P is in x
@@ -39,6 +49,7 @@ struct Params {
     int workers;
     float* tail_ws;
     int tail_min;
+    TailRule tail_rule;
     unsigned long long timeout_ns;
     int* status;
 };
@@ -183,7 +194,7 @@ struct Walk {
             plan->u = plan->end = 0;
             plan->share = 1;
             const int rest = items % p.workers;
-            if (p.tail_ws != nullptr && rest != 0 && 10 * rest < 9 * p.workers) {
+            if (p.tail_ws != nullptr && rest != 0) {
                 int longest = plan->blocks;
                 int64_t all = static_cast<int64_t>(rest) * plan->blocks;
                 if (!UNIFORM) {
@@ -196,7 +207,9 @@ struct Walk {
                     }
                 }
                 const int64_t share = max(static_cast<int64_t>(p.tail_min), (all + p.workers - 1) / p.workers);
-                if (all <= (1 << 30) && share < longest) {
+                const TailRule& r = p.tail_rule;
+                const int price = 2 * rest <= p.workers ? r.base + r.slope * rest / p.workers : r.over;
+                if (all <= (1 << 30) && longest - share >= max(1, price)) {
                     plan->share = static_cast<int>(share);
                     plan->full = items - rest;
                     plan->u = static_cast<int>(min(all, me * share));

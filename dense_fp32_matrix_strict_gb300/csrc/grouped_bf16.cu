@@ -29,6 +29,7 @@
 // accumulators of 256 columns, so the epilogue of one tile runs beside the
 // MMAs of the next.
 #include <atomic>
+#include <climits>
 #include <cstring>
 
 #include "grouped.cuh"
@@ -714,6 +715,14 @@ Tail bf16_tail(const Params& p, bool wgrad, const DeviceInfo* dev) {
     // 1024 x 1024: 15.1 us whole, 18.0 in halves; 1 x 64 rows, 4096 x 4096:
     // 32.2 whole, 21.1 in quarters).
     t.worth = 32;
+    // A slot's bytes grow with a tile's rows, and W of many pairs comes at HBM's
+    // rate whether they share tiles or not (K = 8192, us whole and cut: 4 tiles
+    // of 32 rows 58 and 22, of 256 rows 46 and 27; 32 tiles of 32 rows 58 and
+    // 49, of 256 rows 56 and 58; 60 tiles of 32 rows 66 and 77, of 256 rows 68
+    // and 88). Tiles of more than 160 rows never gained above a half.
+    const int64_t mean = wgrad ? p.K : p.rows / used;
+    const int high = static_cast<int>(mean < TILE ? mean : TILE);
+    t.rule = TailRule{10, 35 + high * high / 800, high <= 160 ? 55 + high / 8 : INT_MAX};
     return t;
 }
 
@@ -752,6 +761,7 @@ cudaError_t launch_bf16(const Params& p0, bool wgrad, const DeviceInfo* dev, cud
     if (p.tail_ws == nullptr && t.items < workers) workers = t.items;
     p.workers = static_cast<int>(workers);
     p.tail_min = static_cast<int>(t.min_blocks);
+    p.tail_rule = t.rule;
     cudaError_t e = launch_kernel(kernel, dim3(static_cast<unsigned>(2 * workers)), dim3(threads_of(wgrad)),
                                   SMEM_FIXED + sched, stream, p.pdl != 0, 2, a, b, b64, b32, b16, p);
     if (e == cudaSuccess && p.tail_ws != nullptr) {

@@ -529,6 +529,7 @@ cudaError_t launch_tile(const Params& p0, const Tail& t, const DeviceInfo* dev, 
     const int64_t workers = p.tail_ws == nullptr && t.items < t.workers ? t.items : t.workers;
     p.workers = static_cast<int>(workers);
     p.tail_min = static_cast<int>(t.min_blocks);
+    p.tail_rule = t.rule;
     cudaError_t e = launch_kernel(tile_kernel<MODE, BM, B_TMA>, dim3(static_cast<unsigned>(workers)),
                                   dim3(threads_of(BM)), smem_fixed(BM) + sched, stream, p.pdl != 0, 1, a, b, p);
     if (e == cudaSuccess && p.tail_ws != nullptr)
@@ -553,6 +554,11 @@ Tail f32_tail(const Params& p, bool wgrad, const DeviceInfo* dev) {
     t.blocks = ((wgrad ? p.rows / used : p.K) + BK - 1) / BK;
     t.min_blocks = bm == 32 ? 8 : 3;
     t.worth = bm == 32 ? 16 : 6;                      // about 10 us
+    // Whole and cut, us: 8 tiles of 128 rows, K = 256, 33 and 27, K = 4096, 361
+    // and 45; 136 of 152 tiles, K = 2048, 191 and 194, K = 4096, 365 and 350;
+    // weight gradients over 256 rows, 8 tiles 27 and 24, 64 tiles 28 and 32;
+    // 64 of 304 tiles of 32 rows, K = 1024, 33 and 26, 272 tiles 56 and 62.
+    t.rule = bm == 32 ? TailRule{7, 3, 8} : wgrad ? TailRule{4, 4, 12} : TailRule{3, 2, 8};
     return t;
 }
 

@@ -21,9 +21,11 @@ int skinny_parts(const Params& p, const DeviceInfo* dev);
 
 // What a tile kernel's last round is about: workers, tiles (an upper bound:
 // the groups' sizes are not known), blocks of k of a sum (the mean), fewest to
-// a piece, fewest worth cutting; bytes of a slot.
+// a piece, fewest worth a second kernel; when a round is then cut (see
+// TailRule); bytes of a slot.
 struct Tail {
     int64_t workers = 0, items = 0, blocks = 0, min_blocks = 0, worth = 0;
+    TailRule rule;
     size_t slot_bytes = 0;
 };
 Tail bf16_tail(const Params& p, bool wgrad, const DeviceInfo* dev);
