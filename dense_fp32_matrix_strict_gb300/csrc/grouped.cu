@@ -158,7 +158,10 @@ __global__ void __launch_bounds__(256) join_kernel(const float* __restrict__ ws,
 // Mean rows per group up to which float takes the streaming kernel (against
 // 32-row tiles; 32 groups of 10, 2048 x 2048, W stored N x K: 199 and 212 us,
 // of 12: 209 and 211, uneven groups and unaligned W sooner; W stored K x N, of
-// 9: 184 and 171).
+// 9: 184 and 171). The mean is all that the host knows: where one group holds
+// most rows, W is read once for every 8 of them (1024 rows, 2048 x 2048, all in
+// one of 128 groups: 414 us stored N x K, 380 K x N, from L2; a call with that
+// group alone takes tiles, 178 and 155).
 constexpr int64_t skinny_rows(int opw) { return opw ? 10 : 8; }
 // Rounds of tiles from which on the last one is left as it is: cutting it
 // gains half a round in the mean and costs a second kernel.

@@ -66,11 +66,15 @@ constexpr unsigned long long LAND_NS = 20000000ull;
 // STATUS_BAD_INDEX, so no later address depends on it. All threads call it;
 // ends synchronised.
 //
-// Blocks take items round robin, forth and back (item_of): with the costly
-// groups first, every round hands out items of nearly one cost and the last
-// ones are the cheapest, which is as good as a work queue without its counter.
-// Above kSortGroups groups there are many items per block and the order is
-// left as it is (the ranking is quadratic).
+// Blocks take items round robin, forth and back (item_of), large groups first:
+// a work queue's balance, nearly, without its counter. Groups are sorted, not
+// tiles: a group's tiles are of one height, or its last one is lower, and the
+// heights of neighbouring groups differ (256 rows make one tile of 256, 259 two
+// of 160), so a round's items are not all of one cost. By the tiles' heights
+// the busiest of 76 pairs has 4.4 % more than the mean (16384 rows over 8 uneven
+// groups, 14336 columns) or 8.3 % (8192 rows over 32, 4096 columns). Above
+// kSortGroups groups there are many items per block and the order is left as it
+// is (the ranking is quadratic).
 constexpr int kSortGroups = 256;
 
 struct Schedule {

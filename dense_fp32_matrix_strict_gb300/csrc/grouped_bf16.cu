@@ -13,7 +13,8 @@
 //     elements of an output row and nothing is transposed on the way out.
 // Operands come in by TMA with the 128-byte swizzle in the layout they have:
 // K-major (64 k of a row in 128 bytes) or MN-major (64 columns of a k), the
-// descriptors tell the MMA which. No operand is ever copied or transposed.
+// descriptors tell the MMA which: nothing is transposed. (An operand whose base
+// or strides TMA cannot take arrives as an aligned copy, made before.)
 //
 // Roles per CTA: warp 0 TMA producer, warp 1 (of rank 0) MMA issuer, the next
 // eight or sixteen epilogue, and in the weight gradient one more: its sums run
@@ -46,7 +47,11 @@ constexpr int STAGE_BYTES = 2 * OP_BYTES;
 constexpr int BOX_BYTES = OP_BYTES / 2;               // 64 columns x 64 k, MN-major
 constexpr int TMEM_COLS = 2 * TILE;
 constexpr int ROW_STEP = 32;                          // N extent granule of a pair
-constexpr int BAND = 8;                               // row tiles that share a pass over the columns
+// Row tiles that share a pass over the columns. More keep too many rows in L2
+// (2 uneven groups of 4096 rows in all, 4096 x 14336: 315 us, bands of 16 352,
+// of 32 362), fewer read W more often (8 x 2048 rows, 14336 x 4096: 1043, bands
+// of 2 1100, of 1 1221).
+constexpr int BAND = 8;
 // Epilogue warps. The weight gradient's tiles are short (a group's rows over
 // 64 blocks) and large (FP32 out), its epilogue is what they wait for, and that
 // is a chain of latencies: twice the warps (202 against 224 us, 32 experts of
