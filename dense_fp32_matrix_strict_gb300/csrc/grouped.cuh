@@ -157,9 +157,9 @@ __device__ __forceinline__ int item_of(int r, int w, int workers) {
 
 // What a worker does, tile by tile: whole tiles in rounds, then its share of
 // the last round. When the tiles do not fill the last round (or the only
-// one), its blocks of k, all tiles' in a row, are cut into equal shares: a
-// worker takes the end of one tile, perhaps whole ones, and the start of
-// another. The sums of cut tiles go to slots (2 w: a piece that starts inside
+// one) and TailRule finds it worth it, its blocks of k, all tiles' in a row,
+// are cut into equal shares: a worker takes the end of one tile, perhaps whole
+// ones, and the start of another. The sums of cut tiles go to slots (2 w: a piece that starts inside
 // its tile, 2 w + 1: one that starts with it), and a second kernel adds a
 // tile's pieces in the order of k. Every worker, and that kernel, computes the
 // same cut from the offsets.

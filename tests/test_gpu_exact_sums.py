@@ -145,3 +145,47 @@ def test_grouped_weight_gradients(sizes, M, N, shift, dtype, out):
             if beta == 0 and n > 0:
                 shows_every_block(lambda lo, hi: pd[lo:hi].t() @ qd[lo:hi], n, 32, ot)
             at += n
+
+
+@pytest.mark.parametrize("dtype,sizes,N,K", [
+    # Tiles for 90 % of the workers, sums below and above what cutting the round costs,
+    ("float32", [128] * 8, 2176, 1024), ("float32", [128] * 8, 2176, 4096),
+    # for half and three quarters of them in 32-row tiles,
+    ("float32", [40] * 4, 2432, 2048), ("float32", [40] * 6, 2432, 1024), ("float32", [40, 39, 41, 70], 2432, 600),
+    # for more than half of the pairs, low tiles and tall ones, and after whole rounds.
+    ("bfloat16", [32] * 4, 2816, 16384), ("bfloat16", [256] * 4, 2816, 4096), ("bfloat16", [70, 256, 31, 200], 5632, 4096),
+], ids=str)
+def test_last_rounds_whole_and_cut(dtype, sizes, N, K):
+    torch = _torch()
+    dt = getattr(torch, dtype)
+    gen = torch.Generator(device="cuda").manual_seed(N + K)
+
+    def integers_of(*shape, most):
+        return torch.randint(-most, most + 1, shape, generator=gen, device="cuda").to(dt)
+
+    x, w = integers_of(sum(sizes), K, most=1), integers_of(len(sizes), N, K, most=2)
+    y = torch.full((sum(sizes), N), float("nan"), device="cuda", dtype=dt)
+    sg.sgemm_grouped_tensors(1.0, x, w, offsets_of(sizes), 0.0, y, transw=True)
+    sg.check_status()
+    at = 0
+    for e, n in enumerate(sizes):
+        ref = x[at:at + n].double() @ w[e].double().t()
+        assert torch.equal(y[at:at + n], ref.to(dt))
+        at += n
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("sizes,M,N", [([256, 256], 1024, 1024), ([2048, 100], 1024, 1536), ([300, 0, 2500], 1000, 2000)],
+                         ids=str)
+def test_last_rounds_of_weight_gradients_whole_and_cut(dtype, sizes, M, N):
+    torch = _torch()
+    dt = getattr(torch, dtype)
+    gen = torch.Generator(device="cuda").manual_seed(M + N)
+    p, q = (torch.randint(-1, 2, (sum(sizes), n), generator=gen, device="cuda").to(dt) for n in (M, N))
+    d = torch.full((len(sizes), M, N), float("nan"), device="cuda")
+    sg.sgemm_grouped_wgrad_tensors(1.0, p, q, offsets_of(sizes), 0.0, d)
+    sg.check_status()
+    at = 0
+    for e, n in enumerate(sizes):
+        assert torch.equal(d[e], (p[at:at + n].double().t() @ q[at:at + n].double()).float())
+        at += n
