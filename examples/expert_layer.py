@@ -5,7 +5,7 @@ backward for training, and single-token decode with 4-bit weights.
     weights, experts, offsets, order, place        sgemm_route
     h = x[token of each row] @ up[e].T             sgemm_grouped
     y = relu(h) @ down[e].T                        sgemm_grouped
-    out[t] = sum_j weights[t, j] * y[place[t, j]]
+    out[t] = sum_j weights[t, j] * y[place[t, j]]      over the choices with an expert
 
 Nothing waits for the device between the calls: the sizes of the groups stay
 there. Torch does the gathers, the activation and the weighted sums. Run it

@@ -306,7 +306,8 @@ SGEMM_API int sgemm_clear_shape_configs(void);
  * sgemm_set_wait_timeout_ns — limit on every bounded wait inside the
  * kernels launched after this call, on an mbarrier or on another CTA's flag
  * (default 2e9 ns). Values below 1000 ns are rejected with
- * SGEMM_ERR_INVALID_VALUE.
+ * SGEMM_ERR_INVALID_VALUE. A block of a grouped product sees its copies land
+ * before it ends, for 20 ms where the limit is shorter.
  */
 SGEMM_API int sgemm_set_wait_timeout_ns(uint64_t ns);
 
